@@ -447,10 +447,16 @@ cql_status cql_fp8_dequantize(const void* matrix, uint64_t matrix_bytes, int64_t
  * tokens that the product kernel quantises them on the way.  Host only. */
 cql_status cql_fp8_workspace_size(int32_t k_in, int32_t experts, int32_t tokens, uint64_t* bytes);
 
-/* Reads before the previous kernel completes.  As in the forward above, the
- * kernel immediately before an FP8 forward on its stream must not write the
- * weight: the forward may read it before that kernel has completed.  After
- * cql_fp8_quantize (or any other work in between) a forward is safe. */
+/* Reads before the previous kernels complete.  The forwards' kernels are
+ * launched programmatically dependent, let what follows them start early, and
+ * read the weight (nothing else) before the kernels in front are complete.  So
+ * between a kernel that writes a weight and the first forward that reads it
+ * there must be, on the stream, an ordinary operation: a kernel, copy or memset
+ * that starts after the work before it is complete and does not let its
+ * successor start early.  Another forward of this library is none.
+ * cql_fp8_quantize needs nothing in between: its blocks write through to L2
+ * before they end, a forward right after it starts when they have ended, and
+ * reads the weight from L2. */
 
 /* y [tokens][n_out] = Xq Wq^T.
  *   weight    block-scaled matrix of n_out rows and k_in columns.

@@ -612,8 +612,10 @@ class _Fp8Layer:
     ``out`` is given) output memory comes from torch's allocator on the call's
     stream, so calls may overlap on several streams and be captured.
 
-    The kernel right before a forward on its stream must not write the layer's
-    weight buffer (``include/cql.h``); making the layer is safe after any."""
+    A forward reads the weight before the kernels in front of it are complete:
+    after a kernel that writes the layer's weight buffer (other than
+    ``cql_fp8_quantize``), some operation that is not a forward has to come first
+    on the stream (``include/cql.h``).  Making the layer contains one."""
 
     def __init__(self, weight, n_experts: int, n_out: int, stream=None):
         import torch

@@ -131,9 +131,10 @@ __global__ void __launch_bounds__(Q_WARPS * 32) k_fp8_quantize(Fp8Shape s, const
   }
   if (P::N == 2) word |= __shfl_xor_sync(0xffffffffu, word, 16);
   if (lane == 0) *reinterpret_cast<uint32_t*>(dst + s.scales_off + ((int64_t)quad * s.rows + row) * 4) = word;
-  // A forward that follows directly may read weights before this kernel has
-  // formally completed (its CTAs have exited by then): the codes are in L2, and
-  // the copies of that kernel, which go through the async proxy, see them.
+  // A forward that follows directly may read this matrix as its weight before its
+  // own wait.  Its CTAs start when all of this kernel's have ended, each behind
+  // these fences: every byte is in L2 by then.  It reads codes (through the async
+  // proxy) and weight scales there, past L1, which it must not trust before the wait.
   if (pdl == kFp8Plain) {
     asm volatile("fence.proxy.async.global;" ::: "memory");
     __threadfence();

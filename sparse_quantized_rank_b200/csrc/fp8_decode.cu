@@ -280,9 +280,9 @@ __global__ void __launch_bounds__(DC_THREADS, 2)
       const uint32_t* ws = p.wscale + (int64_t)t.expert * p.n + n0;
       auto weight_scales = [&](int c, uint32_t(&v)[4]) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)               // rows past the expert's last: any finite scale
+        for (int j = 0; j < 4; ++j)               // rows past the expert's last: any finite scale.  From L2: see k_fp8_quantize
           v[j] = c <= c1 && n0 + 32 * j < p.n && CQL_IN(p.status, ws - p.wscale + (int64_t)c * p.wrows + 32 * j, p.in.wscale, 411)
-                     ? __ldg(ws + (int64_t)c * p.wrows + 32 * j)
+                     ? ld_cg_u32(ws + (int64_t)c * p.wrows + 32 * j)
                      : 0x7F7F7F7Fu;
       };
       uint32_t next[4];                           // the next chunk's, on their way

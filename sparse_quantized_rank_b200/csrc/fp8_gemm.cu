@@ -350,10 +350,10 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)             // rows past the expert's last: any finite scale
+          for (int j = 0; j < 4; ++j)             // rows past the expert's last: any finite scale.  From L2: see k_fp8_quantize
             w[i][j] = c + i <= c1 && n0 + 32 * j < p.n &&
                               CQL_IN(p.status, ws - p.wscale + (int64_t)(c + i) * p.wrows + 32 * j, p.in.wscale, 421)
-                          ? __ldg(ws + (int64_t)(c + i) * p.wrows + 32 * j)
+                          ? ld_cg_u32(ws + (int64_t)(c + i) * p.wrows + 32 * j)
                           : 0x7F7F7F7Fu;
 #pragma unroll
           for (int j = 0; j < 8; ++j)

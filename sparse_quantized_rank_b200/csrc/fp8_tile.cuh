@@ -180,15 +180,16 @@ struct F8Tile {
 };
 
 // Tokens [offsets[e], offsets[e+1]) of an expert; a pair that does not lie in
-// order within [0, tokens] is an empty expert (and an error: false).
+// order within [0, tokens] is an empty expert (and an error: false).  Read past L1:
+// the kernels before are done, but a launch that starts early says so only by its wait.
 CQL_DEV bool f8_segment(const F8Tokens& p, int e, int& t0, int& t1) {
   if (p.offsets == nullptr) {
     t0 = 0;
     t1 = p.tokens;
     return true;
   }
-  t0 = p.offsets[e];
-  t1 = p.offsets[e + 1];
+  t0 = __ldcg(p.offsets + e);
+  t1 = __ldcg(p.offsets + e + 1);
   if (t0 >= 0 && t0 <= t1 && t1 <= p.tokens) return true;
   t0 = t1 = 0;
   return false;
