@@ -181,12 +181,14 @@ enum {
 #define CQL_FLAG_NO_MAIN 0x1u
 #define CQL_FLAG_NO_CSR 0x2u
 #define CQL_FLAG_NO_LOWRANK 0x4u
-/* Test only: the tensor-core decode skips loading x, so that its bounded
+/* Test only: the tensor-core decode (and an FP8 forward, where the flag is ORed
+ * into x_dt) skips loading x, so that its bounded
  * waits on x run out (after ~10 ms instead of seconds); the call then
  * completes with CQL_ERR_TIMEOUT in the device error word and y undefined.
  * No copy or MMA is left in flight: nothing that waits on x has started any.
  * As after any device error, the workspace must be initialised again
- * (cql_workspace_init) before its next use. */
+ * (cql_workspace_init) before its next use; those of the FP8 forwards hold
+ * nothing that has to be. */
 #define CQL_FLAG_DEBUG_SKIP_X 0x100u
 /* Decode on the CUDA cores even where the tensor-core decode applies (2:4
  * int4 and int3 layers); for comparing the two designs on the same layer. */

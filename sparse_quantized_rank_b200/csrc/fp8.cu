@@ -261,6 +261,8 @@ cql_status forward(int32_t n_out, int32_t k_in, int32_t experts, const void* wei
   if (experts < 1 || experts > CQL_FP8_MAX_EXPERTS || (int64_t)experts * n_out > (int64_t)CQL_FP8_MAX_ROWS)
     return CQL_ERR_ARG;
   if (tokens < 0 || tokens > CQL_FP8_MAX_TOKENS) return CQL_ERR_ARG;
+  const bool debug = ((uint32_t)x_dt & CQL_FLAG_DEBUG_SKIP_X) != 0;
+  x_dt = (cql_dtype)((uint32_t)x_dt & ~CQL_FLAG_DEBUG_SKIP_X);
   const bool kept = x_dt == CQL_DT_FP8_BLOCK;
   if (!kept && !plain_dt(x_dt)) return CQL_ERR_ARG;
   if (!plain_dt(y_dt)) return CQL_ERR_ARG;
@@ -301,6 +303,7 @@ cql_status forward(int32_t n_out, int32_t k_in, int32_t experts, const void* wei
   p.ydt = (int)y_dt;
   p.ldy = ldy;
   p.status = status;
+  p.debug = debug;
   // an x that is quantised on the way is one of fp8_decodes' too
   return of_cuda(fp8_decodes(tokens, experts, (int64_t)n_out * k_in) ? launch_fp8_decode(p, st)
                                                                     : launch_fp8_gemm(p, st));

@@ -49,6 +49,7 @@ struct Fp8Product {
   int ydt;
   int64_t ldy;
   uint32_t* status;
+  bool debug;                                // x is withheld, the waits for it run out after ~10 ms
 };
 // Elements from a matrix's first to behind its last, rows ld apart.
 inline uint64_t fp8_extent(int64_t rows, int64_t ld, int cols) { return (uint64_t)((rows - 1) * ld + cols); }

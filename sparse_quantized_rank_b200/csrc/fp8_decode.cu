@@ -30,8 +30,10 @@
 //   warps 2..5 x and scales
 //   warps 6..9 epilogue (lane = row of W: a warp stores 32 consecutive outputs
 //              of a token)
-// Every mbarrier wait is bounded; on expiry the kernel records CQL_ERR_TIMEOUT,
-// waits for its own copies and MMAs, and winds down.
+// Every mbarrier wait is bounded; on expiry the kernel records CQL_ERR_TIMEOUT
+// (detail 40 weights, 41 MMA, 42 x and scales, 43 epilogue), waits for its own
+// copies and MMAs, and winds down.  A role that copies ends when all that it has
+// copied is multiplied: no copy and no commit is under way when a CTA ends.
 //
 // Measured (bf16, calls in a chain, weights not in L2): 11008 x 4096, one token
 // 10.2 us for 45.5 MB, 68 % of the copy bandwidth, reading exactly the weights'
@@ -64,6 +66,7 @@ struct DcParams {
   int cols, vec;
   int n, units, row_tiles, stages, split;
   int early;                                      // weights and offsets may be read before the kernel before is done
+  int debug;                                      // x is withheld, the waits are short
   uint32_t tmem_cols;
   void* y;
   int ydt, yvec;                                  // yvec: rows of y are 16-byte aligned
@@ -143,6 +146,7 @@ __global__ void __launch_bounds__(DC_THREADS, 2)
   const int rank = p.split > 1 ? (int)cluster_rank() : 0;
   const int u0 = (int)((int64_t)p.units * rank / p.split), u1 = (int)((int64_t)p.units * (rank + 1) / p.split);
   const int first = p.split > 1 ? (int)blockIdx.x / p.split : (int)blockIdx.x;
+  bool failed = false;                            // the epilogue's waits ran out
   // units of the first tile whose copies start before anything else is set up
   const int tt = (p.tok.tokens + NT - 1) / NT;    // token tiles of a row tile, where there is one expert
   const int ahead = early && p.tok.offsets == nullptr && first < p.row_tiles * tt ? min(p.stages, u1 - u0) : 0;
@@ -195,7 +199,7 @@ __global__ void __launch_bounds__(DC_THREADS, 2)
     if (elect_one()) {
       // ---------------- TMA producer ----------------
       Ring at{0, 0};
-      uint64_t lim = kF8Limit;
+      uint64_t lim = f8_limit(p.debug);
       int done = ahead;
       for (int i = 0; i < ahead; ++i) at.next(p.stages);
       for (int id = first; id < tiles && lim != 0; id += step) {
@@ -203,16 +207,18 @@ __global__ void __launch_bounds__(DC_THREADS, 2)
         const int row = t.expert * p.n + t.rt * kF8Rows;
         for (int u = u0 + done; u < u1; ++u) {
           f8_wait(&S.empty[at.s], at.phase ^ 1, lim);
-          mbar_expect_tx(&S.full[at.s], STAGE);
-          tma_load_3d(ring + (uint32_t)at.s * STAGE, &tmW, &S.full[at.s], 0, row, U * u);
-          at.next(p.stages);
+          const uint32_t on = lim != 0;
+          expect_if(on ? STAGE : 0u, &S.full[at.s]);
+          tma_load_3d_if(on, ring + (uint32_t)at.s * STAGE, &tmW, &S.full[at.s], 0, row, U * u);
+          at.next_if(on, p.stages);
         }
         done = 0;
       }
+      for (int i = 0; i < p.stages; ++i) f8_wait(&S.empty[i], at.last(i), lim);
       if (lim == 0) {
         set_error(p.status, CQL_ERR_TIMEOUT, 40);
-        uint64_t more = kF8Limit;                 // copies in flight
-        for (int i = 0; i < p.stages; ++i) f8_wait(&S.full[i], at.phase ^ (i < at.s ? 0u : 1u), more);
+        uint64_t more = f8_limit(p.debug);       // copies in flight
+        for (int i = 0; i < p.stages; ++i) f8_wait(&S.full[i], at.last(i), more);
       }
     }
   } else if (warp == 1) {
@@ -222,7 +228,7 @@ __global__ void __launch_bounds__(DC_THREADS, 2)
       const uint64_t desc_a = smem_desc_sw128(smem_u32(ring)), desc_x = smem_desc_sw128(smem_u32(xs));
       uint32_t gc = 0;
       Ring at{0, 0}, xat{0, 0};
-      uint64_t lim = kF8Limit;
+      uint64_t lim = f8_limit(p.debug);
       for (int id = first; id < tiles && lim != 0; id += step) {
         int chain = u0;                           // where the next accumulator chain starts
         uint32_t acc = 0;                         // the accumulator holds a sum already
@@ -240,18 +246,19 @@ __global__ void __launch_bounds__(DC_THREADS, 2)
           for (int kk = 0; kk < 4 * U; ++kk)
             mma_f8(d, da + (kk >> 2) * (kF8ABytes >> 4) + 2 * (kk & 3), db + (kk >> 2) * (X_BLOCK >> 4) + 2 * (kk & 3),
                    idesc | f8_byte(U * u + (kk >> 2)), sfa, sfa + 4, kk == 0 ? acc : 1u);
-          commit_if(1u, &S.empty[stage]);
+          commit_if(lim != 0, &S.empty[stage]);
           acc = 1;
         };
         for (int u = u0; u < u1;) {               // a chunk at a time
           const int end = min(u1, (u | (4 / U - 1)) + 1);
           f8_wait_if(u == chain, &S.dempty[gc & 1], ((gc >> 1) & 1) ^ 1, lim);
           f8_wait(&S.xfull[xat.s], xat.phase, lim);
+          if (lim == 0) break;
           for (; u < end; ++u) unit(u);
-          commit_if(1u, &S.xempty[xat.s]);
+          commit_if(lim != 0, &S.xempty[xat.s]);
           xat.next(DC_XSLOTS);
           const uint32_t over = u == f8_chain_end<U>(chain, u1);
-          commit_if(over, &S.dfull[gc & 1]);
+          commit_if(over & (lim != 0), &S.dfull[gc & 1]);
           gc += over;
           acc ^= over;
           chain = over ? u : chain;
@@ -259,7 +266,7 @@ __global__ void __launch_bounds__(DC_THREADS, 2)
       }
       if (lim == 0) {
         set_error(p.status, CQL_ERR_TIMEOUT, 41);
-        uint64_t more = kF8Limit;
+        uint64_t more = f8_limit(p.debug);
         commit_if(1u, &S.drain);                  // MMAs in flight
         f8_wait(&S.drain, 0, more);
       }
@@ -272,9 +279,9 @@ __global__ void __launch_bounds__(DC_THREADS, 2)
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     uint32_t sc = 0;
     Ring at{0, 0};
-    uint64_t lim = kF8Limit;
-    bool waited = !early;
-    for (int id = first; id < tiles && __all_sync(0xffffffffu, lim != 0); id += step) {
+    uint64_t lim = f8_limit(p.debug);
+    bool waited = !early, ok = true;
+    for (int id = first; id < tiles && ok; id += step) {
       const F8Tile t = f8_tile(p.tok, map, p.row_tiles, id);
       const int n0 = t.rt * kF8Rows + lane, cnt = t.t1 - t.t0, c0 = U * u0 >> 2, c1 = (U * u1 - 1) >> 2;
       const uint32_t* ws = p.wscale + (int64_t)t.expert * p.n + n0;
@@ -316,7 +323,9 @@ __global__ void __launch_bounds__(DC_THREADS, 2)
         if constexpr (DT < 0) {
           if (c < c1) token_scale(c + 1);
           f8_wait(&S.xempty[at.s], at.phase ^ 1, lim);
-          if (q == 0 && elect_one()) {
+          ok = __all_sync(0xffffffffu, lim != 0);
+          if (!ok) break;
+          if (q == 0 && p.debug == 0 && elect_one()) {
             mbar_expect_tx(&S.xfull[at.s], X_SLOT);
             tma_load_3d(slot, &tmX, &S.xfull[at.s], 0, t.t0, 4 * c);
           }
@@ -332,6 +341,8 @@ __global__ void __launch_bounds__(DC_THREADS, 2)
           Raw raw = ahead_x;
           fetch_x(c + 1, (q + c + 1) & 3, ahead_x);
           f8_wait(&S.xempty[at.s], at.phase ^ 1, lim);
+          ok = __all_sync(0xffffffffu, lim != 0);
+          if (!ok) break;
           for (int k = (q + c) & 3; k < cnt; k += 4) {
             uint32_t byte;
             const uint4 w = quantize16<XDT>(raw, byte);
@@ -353,6 +364,8 @@ __global__ void __launch_bounds__(DC_THREADS, 2)
         tmem_st4(sf, v);
         if constexpr (DT >= 0) {
           f8_wait(&S.xbytes[sc & 1], (sc >> 1) & 1, lim);
+          ok = __all_sync(0xffffffffu, lim != 0);
+          if (!ok) break;
           if (lane < cnt) xword = *reinterpret_cast<const uint32_t*>(S.byte[sc & 1][lane]);
           __syncwarp();
         }
@@ -360,15 +373,20 @@ __global__ void __launch_bounds__(DC_THREADS, 2)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.xfull[at.s]);
+        if (lane == 0 && (DT < 0 || p.debug == 0)) mbar_arrive(&S.xfull[at.s]);
       }
     }
-    if (lim == 0 && lane == 0) set_error(p.status, CQL_ERR_TIMEOUT, 42);
+    for (int s = 0; s < DC_XSLOTS; ++s) f8_wait(&S.xempty[s], at.last(s), lim);
+    if (!__all_sync(0xffffffffu, lim != 0)) {
+      if (lane == 0) set_error(p.status, CQL_ERR_TIMEOUT, 42);
+      uint64_t more = f8_limit(p.debug);         // copies of x in flight
+      for (int s = 0; DT < 0 && s < DC_XSLOTS; ++s) f8_wait(&S.xfull[s], at.last(s), more);
+    }
   } else {
     // ---------------- epilogue ----------------
     const int q = warp & 3, row = 32 * q + lane;
     uint32_t gc = 0;
-    uint64_t lim = kF8Limit;
+    uint64_t lim = f8_limit(p.debug);
     bool ok = true, pushed = false;
     if (early) pdl_wait();                        // y may be in use by the kernel before
     for (int id = first; id < tiles && ok; id += step) {
@@ -442,6 +460,7 @@ __global__ void __launch_bounds__(DC_THREADS, 2)
       }
     }
     if (!ok && lane == 0) set_error(p.status, CQL_ERR_TIMEOUT, 43);
+    failed = !ok;
     if (p.split > 1 && !pushed) {                 // nothing to push
       cluster_wait();
       cluster_arrive();
@@ -454,6 +473,7 @@ __global__ void __launch_bounds__(DC_THREADS, 2)
       cluster_arrive();
     }
     cluster_wait();                               // no CTA of the cluster pushes to this one any more
+    if (failed) f8_pause();                       // what they have pushed, and this one did not wait for
   }
   tc_fence_before();
   __syncthreads();
@@ -584,6 +604,7 @@ cudaError_t launch_fp8_decode(const Fp8Product& f, cudaStream_t st) {
   p.n = f.n;
   p.row_tiles = (f.n + kF8Rows - 1) / kF8Rows;
   p.early = f.early;
+  p.debug = f.debug;
   p.y = f.y;
   p.ydt = f.ydt;
   p.yvec = (reinterpret_cast<uintptr_t>(f.y) & 15) == 0 && (f.ldy * (f.ydt == CQL_DT_F32 ? 4 : 2)) % 16 == 0;

@@ -24,8 +24,10 @@
 //   warps 4..7  scale words: global -> registers -> tensor memory
 //   warps 8..15 epilogue: partial sums of the segments in registers, one
 //               rounding, a turn through shared memory, 16-byte stores
-// Every mbarrier wait is bounded; on expiry the kernel records CQL_ERR_TIMEOUT,
-// waits for its own copies and MMAs, and winds down.
+// Every mbarrier wait is bounded; on expiry the kernel records CQL_ERR_TIMEOUT
+// (detail 44 copies, 45 MMA, 46 scale words, 47 epilogue), waits for its own copies
+// and MMAs, and winds down.  A role that copies ends when all that it has copied is
+// multiplied: no copy and no commit is under way when a CTA ends.
 //
 // What bounds it.  A block of a 256 x 224 tile is 448 cycles of MMA and 30 KB a
 // CTA, 67 bytes a cycle, about what an SM takes from L2 (copies alone: 19 TB/s
@@ -58,6 +60,7 @@ struct GmParams {
   int64_t wrows;
   int n, units, row_tiles, stages;
   int early;                                      // weights and offsets may be read before the kernel before is done
+  int debug;                                      // x is withheld, the waits are short
   void* y;
   int ydt, yvec;                                  // yvec: rows of y are 16-byte aligned
   int64_t ldy;
@@ -81,14 +84,6 @@ CQL_DEV void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uin
       "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
       : "memory");
 }
-CQL_DEV void expect_if(uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
-      "r"(bytes)
-      : "memory");
-}
 // If `on`: all earlier MMAs done -> an arrival on the barrier in the CTAs of `mask`.
 CQL_DEV void commit_pair_if(uint32_t on, uint64_t* bar, uint16_t mask) {
   asm volatile(
@@ -99,13 +94,15 @@ CQL_DEV void commit_pair_if(uint32_t on, uint64_t* bar, uint16_t mask) {
       "h"(mask), "r"(on)
       : "memory");
 }
-// A copy into this CTA's shared memory whose bytes count on the barrier of the
-// pair's first CTA (the same address with the CTA bit cleared).
-CQL_DEV void tma_load_pair(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+// If `on`: a copy into this CTA's shared memory whose bytes count on the barrier of
+// the pair's first CTA (the same address with the CTA bit cleared).
+CQL_DEV void tma_load_pair_if(uint32_t on, void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
-      "%5}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar) & 0xFEFFFFFFu), "r"(x), "r"(y), "r"(z)
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %6, 0;\n\t"
+      "@p cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+      "%5}], [%2];\n\t}" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar) & 0xFEFFFFFFu), "r"(x), "r"(y), "r"(z), "r"(on)
       : "memory");
 }
 // An arrival on the barrier of the cluster's CTA `rank`.  It orders tensor-memory
@@ -247,22 +244,30 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
       // the pair's bytes, on its first CTA's barrier
       const uint32_t expect = rank == head ? 2 * U * (x ? x_block : kF8ABytes) : 0u;
       const int half = (int)(rank & 1);
+      const uint32_t copies = !x || p.debug == 0;
       Ring at{0, 0};
-      uint64_t lim = kF8Limit;
+      uint64_t lim = f8_limit(p.debug);
       for (int id = first; id < tiles && lim != 0; id += step) {
         const F8Tile t = f8_tile(p.tok, map, p.row_tiles, id);
         const int row = x ? t.t0 + half * (gm_columns(t) >> 1) : t.expert * p.n + (2 * t.rt + half) * kF8Rows;
         for (int u = 0; u < p.units; ++u) {
           f8_wait(&S.empty[at.s], at.phase ^ 1, lim);
-          expect_if(expect, &S.full[at.s]);
-          tma_load_pair(ring + (uint32_t)at.s * stage_bytes + off, tm, &S.full[at.s], 0, row, U * u);
-          at.next(p.stages);
+          const uint32_t on = copies & (lim != 0);
+          expect_if(on ? expect : 0u, &S.full[at.s]);
+          tma_load_pair_if(on, ring + (uint32_t)at.s * stage_bytes + off, tm, &S.full[at.s], 0, row, U * u);
+          at.next_if(on, p.stages);
         }
       }
+      for (int i = 0; i < p.stages; ++i) f8_wait(&S.empty[i], at.last(i), lim);
       if (lim == 0) {
-        set_error(p.status, CQL_ERR_TIMEOUT, 40);
-        uint64_t more = kF8Limit;                 // copies in flight
-        for (int i = 0; i < p.stages; ++i) f8_wait(&S.full[i], at.phase ^ (i < at.s ? 0u : 1u), more);
+        set_error(p.status, CQL_ERR_TIMEOUT, 44);
+        // Copies in flight.  Both CTAs' show on the first one's barriers alone.
+        uint64_t more = f8_limit(p.debug);
+        if (rank == head) {
+          for (int i = 0; i < p.stages; ++i) f8_wait(&S.full[i], at.last(i), more);
+        } else {
+          f8_pause();
+        }
       }
     } else if (warp == 1 && rank == head && elect_one()) {
       // ---------------- MMA issuer ----------------
@@ -274,7 +279,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
       const uint64_t desc0 = smem_desc_sw128(smem_u32(ring));
       uint32_t gc = 0;
       Ring at{0, 0}, sat{0, 0};
-      uint64_t lim = kF8Limit;
+      uint64_t lim = f8_limit(p.debug);
       for (int id = first; id < tiles && lim != 0; id += step) {
         int chain = 0;                            // where the next accumulator chain starts
         uint32_t acc = 0;                         // the accumulator holds a sum already
@@ -293,7 +298,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
             mma_f8_pair(d, da + (kk >> 2) * (kF8ABytes >> 4) + 2 * (kk & 3),
                         db + (uint64_t)((kk >> 2) * (x_block >> 4)) + 2 * (kk & 3), idesc | f8_byte(U * u + (kk >> 2)),
                         sfa, sfa + 4, kk == 0 ? acc : 1u);
-          commit_pair_if(1u, &S.empty[stage], pair);
+          commit_pair_if(lim != 0, &S.empty[stage], pair);
           acc = 1;
         };
         // A chunk at a time (4 / U units): with the waits and commits of a
@@ -302,6 +307,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
           const int end = min(p.units, u + 4 / U);
           f8_wait_if(u == chain, &S.dempty[gc & 1], ((gc >> 1) & 1) ^ 1, lim);
           f8_wait(&S.sfull[sat.s], sat.phase, lim);
+          if (lim == 0) break;
           if (end - u == 4 / U) {
 #pragma unroll
             for (int i = 0; i < 4 / U; ++i) unit(u + i);
@@ -309,10 +315,10 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
           } else {
             for (; u < end; ++u) unit(u);
           }
-          commit_pair_if(1u, &S.sempty[sat.s], pair);
+          commit_pair_if(lim != 0, &S.sempty[sat.s], pair);
           sat.next(GM_SF_SLOTS);
           const uint32_t over = u == f8_chain_end<U>(chain, p.units);
-          commit_pair_if(over, &S.dfull[gc & 1], pair);
+          commit_pair_if(over & (lim != 0), &S.dfull[gc & 1], pair);
           gc += over;
           acc ^= over;
           chain = over ? u : chain;
@@ -323,8 +329,8 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
       // the last ones that come to this CTA.
       for (uint32_t i = gc < 2 ? 0 : gc - 2; i < gc && lim != 0; ++i) f8_wait(&S.dempty[i & 1], (i >> 1) & 1, lim);
       if (lim == 0) {
-        set_error(p.status, CQL_ERR_TIMEOUT, 41);
-        uint64_t more = kF8Limit;
+        set_error(p.status, CQL_ERR_TIMEOUT, 45);
+        uint64_t more = f8_limit(p.debug);
         commit_pair_if(1u, &S.drain, (uint16_t)(1u << head));         // MMAs in flight
         f8_wait(&S.drain, 0, more);
       }
@@ -334,18 +340,19 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     Ring at{0, 0};
-    uint64_t lim = kF8Limit;
+    uint64_t lim = f8_limit(p.debug);
+    bool ok = true;
     if (early) {
       pdl_wait();
       pdl_launch_dependents();
     }
     const int c1 = U * (p.units - 1) >> 2;        // chunks 0 .. c1
-    for (int id = first; id < tiles && __all_sync(0xffffffffu, lim != 0); id += step) {
+    for (int id = first; id < tiles && ok; id += step) {
       const F8Tile t = f8_tile(p.tok, map, p.row_tiles, id);
       const int n0 = (2 * t.rt + (int)(rank & 1)) * kF8Rows + lane;
       const uint32_t* ws = p.wscale + (int64_t)t.expert * p.n + n0;
       const uint32_t* xs = p.xscale + t.t0 + lane;
-      for (int c = 0; c <= c1; c += 4) {
+      for (int c = 0; c <= c1 && ok; c += 4) {
         uint32_t w[4][12];                        // four chunks' words, on their way together
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -366,7 +373,8 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
         for (int i = 0; i < 4; ++i) {
           if (c + i > c1) break;
           f8_wait(&S.sempty[at.s], at.phase ^ 1, lim);
-          __syncwarp();
+          ok = __all_sync(0xffffffffu, lim != 0);
+          if (!ok) break;
           tc_fence_after();
           const uint32_t sf = sf0 + lanes + (uint32_t)at.s * GM_SF_COLS;
           tmem_st4(sf, w[i]);
@@ -380,14 +388,15 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
         }
       }
     }
-    if (lim == 0 && lane == 0) set_error(p.status, CQL_ERR_TIMEOUT, 42);
+    for (int i = 0; i < GM_SF_SLOTS; ++i) f8_wait(&S.sempty[i], at.last(i), lim);
+    if (!__all_sync(0xffffffffu, lim != 0) && lane == 0) set_error(p.status, CQL_ERR_TIMEOUT, 46);
   } else {
     // ---------------- epilogue ----------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     const int q = warp & 3, h = (warp - 8) >> 2;
     uint32_t* buf32 = bounce + (warp - 8) * 256;
     uint32_t gc = 0;
-    uint64_t lim = kF8Limit;
+    uint64_t lim = f8_limit(p.debug);
     bool ok = true;
     if (early) pdl_wait();                        // y may be in use by the kernel before
     for (int id = first; id < tiles && ok; id += step) {
@@ -452,7 +461,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
           if (c < part && c < left) store_tokens16(buf32, acc + c, y + c * p.ldy, left - c, p.ydt, o);
       }
     }
-    if (!ok && lane == 0) set_error(p.status, CQL_ERR_TIMEOUT, 43);
+    if (!ok && lane == 0) set_error(p.status, CQL_ERR_TIMEOUT, 47);
     arrived = ok && first < tiles;
   }
   __syncwarp();
@@ -522,6 +531,7 @@ cudaError_t launch_fp8_gemm(const Fp8Product& f, cudaStream_t st) {
   p.n = f.n;
   p.row_tiles = (f.n + 2 * kF8Rows - 1) / (2 * kF8Rows);
   p.early = f.early;
+  p.debug = f.debug;
   p.y = f.y;
   p.ydt = f.ydt;
   p.yvec = (reinterpret_cast<uintptr_t>(f.y) & 15) == 0 && (f.ldy * (f.ydt == CQL_DT_F32 ? 4 : 2)) % 16 == 0;

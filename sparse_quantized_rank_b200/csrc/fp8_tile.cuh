@@ -18,8 +18,9 @@ constexpr uint32_t kF8ABytes = kF8Rows * 128;     // their codes of one block
 constexpr int kF8Seg = 16;
 
 // Waits for a barrier's phase if `on`; bounded by `lim` clock cycles.  Once a
-// wait has run out, lim is 0 and every further one tries just once, so that a
-// role runs to the end of its tile, where it looks at lim.
+// wait has run out, lim is 0 and every further one tries just once: the role
+// signals nothing and issues no copy any more, so that those which wait for it
+// run out as well, and stops at the next turn where it looks at lim.
 // The loop is written in PTX, without a result to branch on: a wait that finds
 // its phase complete costs the issuing thread about 50 cycles like this, 190
 // where C++ branches on the outcome (measured on single-thread loops; the MMA
@@ -63,7 +64,36 @@ CQL_DEV uint32_t f8_peek(uint64_t* bar, uint32_t parity) {
       : "memory");
   return done;
 }
-constexpr uint64_t kF8Limit = (uint64_t)kTcWaitCycles;
+// debug: a test withholds x to let the waits run out.
+CQL_DEV uint64_t f8_limit(int debug) { return (uint64_t)(debug ? kTcDebugWaitCycles : kTcWaitCycles); }
+// Some 2 ms, for copies from the cluster's other CTAs that no barrier of this one
+// counts any more (after a wait that ran out): their last chance to land.
+constexpr long long kF8Pause = 4000000ll;
+CQL_DEV void f8_pause() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < kF8Pause) {
+  }
+}
+// If bytes > 0: an arrival that expects them.
+CQL_DEV void expect_if(uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(bytes)
+      : "memory");
+}
+
+// If `on`: tma_load_3d.
+CQL_DEV void tma_load_3d_if(uint32_t on, void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %6, 0;\n\t"
+      "@p cp.async.bulk.tensor.3d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::
+          "r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(on)
+      : "memory");
+}
 
 // One lane of a converged warp.
 CQL_DEV bool elect_one() {
@@ -162,6 +192,8 @@ struct Ring {
     s = wrap ? 0 : s;
     phase ^= wrap ? 1u : 0u;
   }
+  // parity of slot i's last round
+  CQL_DEV uint32_t last(int i) const { return phase ^ (i < s ? 0u : 1u); }
 };
 
 // Sizes that the checked build holds indices against: words of the two scale
