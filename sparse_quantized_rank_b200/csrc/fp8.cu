@@ -278,6 +278,7 @@ cql_status forward(int32_t n_out, int32_t k_in, int32_t experts, const void* wei
   p.x = fp8_shape(tokens, k_in);
   p.w_base = static_cast<const uint8_t*>(weight);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool few = fp8_decodes(tokens, experts, (int64_t)n_out * k_in);
   if (kept) {
     p.x_base = static_cast<const uint8_t*>(x);
   } else {
@@ -289,7 +290,9 @@ cql_status forward(int32_t n_out, int32_t k_in, int32_t experts, const void* wei
       if (workspace == nullptr) return CQL_ERR_ARG;
       if (!aligned_to(workspace, 256)) return CQL_ERR_ALIGN;
       if (ws_bytes < p.x.total) return CQL_ERR_SIZE;
-      const cudaError_t e = launch_fp8_quantize(p.x, x, x_dt, ldx, static_cast<uint8_t*>(workspace),
+      cudaError_t e = few ? ready_fp8_decode() : ready_fp8_gemm();    // before anything is launched
+      if (e != cudaSuccess) return CQL_ERR_CUDA;
+      e = launch_fp8_quantize(p.x, x, x_dt, ldx, static_cast<uint8_t*>(workspace),
                                                 offsets == nullptr ? kFp8Early : kFp8Offsets, st);
       if (e != cudaSuccess) return CQL_ERR_CUDA;
       p.x_base = static_cast<const uint8_t*>(workspace);
@@ -305,8 +308,7 @@ cql_status forward(int32_t n_out, int32_t k_in, int32_t experts, const void* wei
   p.status = status;
   p.debug = debug;
   // an x that is quantised on the way is one of fp8_decodes' too
-  return of_cuda(fp8_decodes(tokens, experts, (int64_t)n_out * k_in) ? launch_fp8_decode(p, st)
-                                                                    : launch_fp8_gemm(p, st));
+  return of_cuda(few ? launch_fp8_decode(p, st) : launch_fp8_gemm(p, st));
 }
 
 }  // namespace

@@ -57,8 +57,10 @@ inline uint64_t fp8_extent(int64_t rows, int64_t ld, int cols) { return (uint64_
 // way, from `raw`; else it is block-scaled already.
 bool fp8_decodes(int tokens, int experts, int64_t weights);           // weights: n_out * k_in of an expert
 bool fp8_decode_quantizes(int tokens, int experts);
+cudaError_t ready_fp8_decode();               // what the launch asks of the runtime succeeds
 cudaError_t launch_fp8_decode(const Fp8Product& p, cudaStream_t st);
 // Any number, X block-scaled (fp8_gemm.cu).
+cudaError_t ready_fp8_gemm();
 cudaError_t launch_fp8_gemm(const Fp8Product& p, cudaStream_t st);
 
 }  // namespace cql

@@ -46,6 +46,7 @@
 // a part of both.
 #include <cuda.h>
 
+#include "fp8_query.h"
 #include "fp8_tile.cuh"
 
 namespace cql {
@@ -488,34 +489,36 @@ constexpr int DC_SMEM = 113 * 1024;               // two CTAs an SM
 // that allocates tensor memory the runtime counts one CTA an SM.
 __global__ void __launch_bounds__(DC_THREADS, 2) k_fp8_decode_size() {}
 
-// How many clusters of `split` CTAs run at once on the current device: a cluster
+// How many clusters of 2 .. 8 CTAs run at once on the current device: a cluster
 // lies within one part of the GPU, so fewer than its CTAs / split.
-int clusters_at_once(int split) {
-  static std::atomic<int> known[64][9];           // by device: one more than the answer, 0 until it was asked
+struct ClustersAtOnce {
+  int n[9];
+};
+cudaError_t clusters_at_once(ClustersAtOnce& c) {
+  static KeptAnswer kept[64][9];                  // by device
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  std::atomic<int>& k = known[dev & 63][split];
-  int n = k.load(std::memory_order_relaxed) - 1;
-  if (n >= 0) return n;
-  n = 0;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)split);
-  cfg.blockDim = dim3(DC_THREADS);
-  cfg.dynamicSmemBytes = DC_SMEM;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = (unsigned)split;
-  at.val.clusterDim.y = 1;
-  at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  if (cudaFuncSetAttribute(k_fp8_decode_size, cudaFuncAttributeMaxDynamicSharedMemorySize, DC_SMEM) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, k_fp8_decode_size, &cfg) != cudaSuccess) {
-    (void)cudaGetLastError();
-    n = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  for (int split = 2; split <= 8; ++split) {
+    e = (cudaError_t)kept[dev & 63][split].get(c.n[split], [split](int& n) {
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3((unsigned)split);
+      cfg.blockDim = dim3(DC_THREADS);
+      cfg.dynamicSmemBytes = DC_SMEM;
+      cudaLaunchAttribute at{};
+      at.id = cudaLaunchAttributeClusterDimension;
+      at.val.clusterDim.x = (unsigned)split;
+      at.val.clusterDim.y = 1;
+      at.val.clusterDim.z = 1;
+      cfg.attrs = &at;
+      cfg.numAttrs = 1;
+      n = 0;
+      const cudaError_t r = cudaFuncSetAttribute(k_fp8_decode_size, cudaFuncAttributeMaxDynamicSharedMemorySize, DC_SMEM);
+      return (int)(r != cudaSuccess ? r : cudaOccupancyMaxActiveClusters(&n, k_fp8_decode_size, &cfg));
+    });
+    if (e != cudaSuccess) return e;
   }
-  k.store(n + 1, std::memory_order_relaxed);
-  return n;
+  return cudaSuccess;
 }
 
 template <int DT, int NT, int U>
@@ -529,14 +532,17 @@ cudaError_t launch(const Fp8Product& f, DcParams& p, cudaStream_t st) {
   const int64_t tiles = tt * p.row_tiles;
   p.units = (f.w.blocks + U - 1) / U;
   static std::atomic<uint64_t> attr_done{0};
-  const cudaError_t e = ensure_smem_attr(attr_done, (const void*)k_fp8_decode<DT, NT, U>, DC_SMEM);
+  cudaError_t e = ensure_smem_attr(attr_done, (const void*)k_fp8_decode<DT, NT, U>, DC_SMEM);
   if (e != cudaSuccess) return e;
   // Split as far as all clusters run at once, with one to spare, and each CTA keeps
   // four blocks.  A second round of clusters costs more than the split gives: 9472 x
   // 4096, one token, 74 clusters of 4 of which 71 run at once 14.2 us, of 3 9.5.
   p.split = 1;
+  ClustersAtOnce at_once;
+  e = clusters_at_once(at_once);
+  if (e != cudaSuccess) return e;
   for (int s = 2; s <= 8 && tiles * s <= 2 * sms && U * p.units >= 4 * s; ++s)
-    if (tiles < clusters_at_once(s)) p.split = s;
+    if (tiles < at_once.n[s]) p.split = s;
   p.tmem_cols = 2 * NT + DC_XSLOTS * DC_SF_COLS <= 64 ? 64 : 128;
   constexpr uint32_t STAGE = U * kF8ABytes;
   const uint32_t xbytes = DC_XSLOTS * 4u * NT * 128u;
@@ -587,6 +593,11 @@ bool fp8_decodes(int tokens, int experts, int64_t weights) {
 // 11008 x 4096, 4 tokens 11.6, 8 tokens 12.4 against 11.7 after a quantise
 // kernel, 16 tokens 16.2 against 12.3.
 bool fp8_decode_quantizes(int tokens, int experts) { return (tokens + experts - 1) / experts <= 4; }
+
+cudaError_t ready_fp8_decode() {
+  ClustersAtOnce at_once;
+  return clusters_at_once(at_once);
+}
 
 cudaError_t launch_fp8_decode(const Fp8Product& f, cudaStream_t st) {
   DcParams p{};

@@ -40,6 +40,7 @@
 // 4096 x 4096, 64 tokens each 92 us, 6.1 TB/s.
 #include <cuda.h>
 
+#include "fp8_query.h"
 #include "fp8_tile.cuh"
 
 namespace cql {
@@ -51,6 +52,7 @@ constexpr int GM_NT = 224;                        // most tokens a tile
 constexpr int GM_ACC = GM_NT / 2;                 // accumulator columns of an epilogue thread
 constexpr int GM_SF_SLOTS = 4;
 constexpr uint32_t GM_SF_COLS = 12;               // a slot: 4 columns of weight scales, up to 8 of token scales
+constexpr int GM_REGS_SUM = 128 * 40 + 128 * 104 + 256 * 176, GM_REGS_DEC = 104;   // setmaxnreg of the roles below
 static_assert(2 * GM_NT + GM_SF_SLOTS * GM_SF_COLS <= 512, "tensor-memory columns");
 
 struct GmParams {
@@ -231,8 +233,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
   const uint32_t sf0 = tmem + 2u * nt;            // scale slots behind the accumulators
   const int first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
 
-  // Register split (128 a thread at launch): 128 * 40 + 128 * 104 + 256 * 176
-  // = 63488 <= 512 * 128.
+  // Register split: GM_REGS_SUM of the 512 * 128 at launch (ready_gemm).
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if ((warp & 1) == 0 && warp < 4 && elect_one()) {
@@ -479,18 +480,34 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
 
 }  // namespace
 
-static int regs_of(const void* f) {
-  cudaFuncAttributes a;
-  return cudaFuncGetAttributes(&a, f) == cudaSuccess ? a.numRegs : 0;
+// The kernel may be launched on the current device, and its registers at launch hold
+// the split that its roles make of them.
+template <int U>
+static cudaError_t ready_gemm() {
+  static std::atomic<uint64_t> attr_done{0};
+  static KeptAnswer kept;
+  cudaError_t e = ensure_smem_attr(attr_done, (const void*)k_fp8_gemm<U>, 227 * 1024);
+  if (e != cudaSuccess) return e;
+  int regs = 0;
+  e = (cudaError_t)kept.get(regs, [](int& n) {
+    cudaFuncAttributes a;
+    const cudaError_t r = cudaFuncGetAttributes(&a, (const void*)k_fp8_gemm<U>);
+    n = r == cudaSuccess ? a.numRegs : 0;
+    return (int)r;
+  });
+  if (e != cudaSuccess) return e;
+  return register_split_fits(regs, GM_THREADS, GM_REGS_SUM, GM_REGS_DEC) ? cudaSuccess : cudaErrorInvalidConfiguration;
+}
+
+cudaError_t ready_fp8_gemm() {
+  const cudaError_t e = ready_gemm<1>();
+  return e != cudaSuccess ? e : ready_gemm<2>();
 }
 
 template <int U>
 static cudaError_t launch_gemm(const Fp8Product& f, GmParams& p, int64_t tiles, cudaStream_t st) {
-  static std::atomic<uint64_t> attr_done{0};
-  const cudaError_t e = ensure_smem_attr(attr_done, (const void*)k_fp8_gemm<U>, 227 * 1024);
+  const cudaError_t e = ready_gemm<U>();
   if (e != cudaSuccess) return e;
-  static const int regs = regs_of((const void*)k_fp8_gemm<U>);        // the register split assumes 128 a thread at launch
-  if (regs != 128) return cudaErrorInvalidConfiguration;
   const int pairs = device_sm_count() / 2, nt = p.tok.nt;
   p.units = (f.w.blocks + U - 1) / U;
   const uint32_t stage = U * (kF8ABytes + (uint32_t)nt * 64u);
