@@ -8,6 +8,8 @@ The checked variant is compiled with -DCQL_CHECKED: every plane read,
 activation read, workspace access and output store of the forward kernels
 is range-checked, and an index outside its buffer records CQL_ERR_RANGE in
 the device error word (the access is skipped) instead of touching memory.
+Quantising and reading back FP8 matrices are checked too; called by
+themselves they have no error word, and skip the access only.
 It stands in for a memory checker on machines where none can run.
 
 The library is compiled straight from ``csrc/*.cu`` with

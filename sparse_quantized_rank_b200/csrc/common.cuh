@@ -68,11 +68,11 @@ CQL_DEV void set_error(uint32_t* err, uint32_t status, uint32_t detail) {
 // Range checks of the checked build (compiled with -DCQL_CHECKED, the
 // library's stand-in for a memory checker): CQL_IN(err, i, n, site) is true
 // when 0 <= i < n; otherwise it records CQL_ERR_RANGE with the site number
-// as the detail and the caller skips the access.  In the normal build it is
-// the constant true and costs nothing.
+// as the detail (with no err, it records nothing) and the caller skips the
+// access.  In the normal build it is the constant true and costs nothing.
 CQL_DEV bool in_range(uint32_t* err, uint64_t i, uint64_t n, uint32_t site) {
   if (i < n) return true;
-  set_error(err, CQL_ERR_RANGE, site);
+  if (err != nullptr) set_error(err, CQL_ERR_RANGE, site);
   return false;
 }
 #ifdef CQL_CHECKED

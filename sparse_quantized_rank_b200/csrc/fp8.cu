@@ -41,7 +41,8 @@ struct Pass {
 // 16 bytes apart within a block, it took 93 us.
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(Q_WARPS * 32) k_fp8_quantize(Fp8Shape s, const void* src, int64_t ld, uint8_t* dst,
-                                                               int pdl) {
+                                                               int pdl, uint32_t* err) {
+  [[maybe_unused]] const uint64_t in_src = fp8_extent(s.rows, ld, s.cols);       // checked build
   using P = Pass<DT, VEC>;
   // The product kernel may start on its weights at once; where it reads offsets
   // too (kFp8Offsets), when the kernels before, which may have written them, are done.
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(Q_WARPS * 32) k_fp8_quantize(Fp8Shape s, const
   for (int i = 0; i < P::N; ++i) {
     const int c = quad * 4 * kGroup + P::col(i, lane);
     const int64_t at = row * ld + c;
-    if (VEC && c + P::PER <= s.cols) {
+    if (VEC && c + P::PER <= s.cols && CQL_IN(err, at + P::PER - 1, in_src, 402)) {
       if constexpr (DT == CQL_DT_F32) {
         const float4 f = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(src) + at);
         v[i][0] = f.x;
@@ -80,7 +81,9 @@ __global__ void __launch_bounds__(Q_WARPS * 32) k_fp8_quantize(Fp8Shape s, const
     } else {
 #pragma unroll
       for (int j = 0; j < P::PER; ++j)
-        v[i][j] = c + j * P::STEP < s.cols ? load_as_f32(src, DT, at + j * P::STEP) : 0.0f;
+        v[i][j] = c + j * P::STEP < s.cols && CQL_IN(err, at + j * P::STEP, in_src, 402)
+                      ? load_as_f32(src, DT, at + j * P::STEP)
+                      : 0.0f;
     }
   }
   // magnitudes compare as integers, infinities and NaNs above every finite one
@@ -112,7 +115,9 @@ __global__ void __launch_bounds__(Q_WARPS * 32) k_fp8_quantize(Fp8Shape s, const
     const float inv = __uint_as_float((254u - (bad ? 127u : byte)) << 23);   // 2^-e
     if (blk < s.blocks) {
       word |= byte << (8 * sub);
-      uint8_t* to = dst + ((int64_t)blk * s.rows + row) * kGroup + (P::col(i, lane) & (kGroup - 1));
+      const int64_t code = ((int64_t)blk * s.rows + row) * kGroup + (P::col(i, lane) & (kGroup - 1));
+      if (!CQL_IN(err, code + (VEC ? P::PER - 1 : 96), s.codes_len, 403)) continue;
+      uint8_t* to = dst + code;
       uint32_t w[P::PER / 4];
 #pragma unroll
       for (int j = 0; j < P::PER / 4; ++j)
@@ -130,7 +135,9 @@ __global__ void __launch_bounds__(Q_WARPS * 32) k_fp8_quantize(Fp8Shape s, const
     }
   }
   if (P::N == 2) word |= __shfl_xor_sync(0xffffffffu, word, 16);
-  if (lane == 0) *reinterpret_cast<uint32_t*>(dst + s.scales_off + ((int64_t)quad * s.rows + row) * 4) = word;
+  const int64_t scale = ((int64_t)quad * s.rows + row) * 4;
+  if (lane == 0 && CQL_IN(err, scale + 3, s.scales_len, 404))
+    *reinterpret_cast<uint32_t*>(dst + s.scales_off + scale) = word;
   // A forward that follows directly may read this matrix as its weight before its
   // own wait.  Its CTAs start when all of this kernel's have ended, each behind
   // these fences: every byte is in L2 by then.  It reads codes (through the async
@@ -150,13 +157,19 @@ __global__ void __launch_bounds__(Q_WARPS * 32) k_fp8_dequantize(Fp8Shape s, con
   const int64_t row = (int64_t)blockIdx.x * Q_WARPS + (threadIdx.x >> 5);
   const int quad = blockIdx.y;
   if (row >= s.rows) return;
-  const uint32_t word = *reinterpret_cast<const uint32_t*>(src + s.scales_off + ((int64_t)quad * s.rows + row) * 4);
+  [[maybe_unused]] uint32_t* const err = nullptr; // the checked build skips, and has no word to record in
+  [[maybe_unused]] const uint64_t in_out = fp8_extent(s.rows, ld, s.cols);
+  const int64_t from_scale = ((int64_t)quad * s.rows + row) * 4;
+  const uint32_t word = CQL_IN(err, from_scale + 3, s.scales_len, 405)
+                            ? *reinterpret_cast<const uint32_t*>(src + s.scales_off + from_scale)
+                            : 0u;
   uint32_t w[P::N][P::PER / 4];
 #pragma unroll
   for (int i = 0; i < P::N; ++i) {
     const int blk = 4 * quad + (P::N == 4 ? i : 2 * i + (lane >> 4));
-    const uint8_t* from = src + ((int64_t)blk * s.rows + row) * kGroup + (P::col(i, lane) & (kGroup - 1));
-    if (blk >= s.blocks) {
+    const int64_t code = ((int64_t)blk * s.rows + row) * kGroup + (P::col(i, lane) & (kGroup - 1));
+    const uint8_t* from = src + code;
+    if (blk >= s.blocks || !CQL_IN(err, code + (VEC ? P::PER - 1 : 96), s.codes_len, 406)) {
 #pragma unroll
       for (int j = 0; j < P::PER / 4; ++j) w[i][j] = 0u;
     } else if constexpr (!VEC) {
@@ -186,7 +199,7 @@ __global__ void __launch_bounds__(Q_WARPS * 32) k_fp8_dequantize(Fp8Shape s, con
     }
     const int c = quad * 4 * kGroup + P::col(i, lane);
     const int64_t at = row * ld + c;
-    if (VEC && c + P::PER <= s.cols) {
+    if (VEC && c + P::PER <= s.cols && CQL_IN(err, at + P::PER - 1, in_out, 407)) {
       if constexpr (DT == CQL_DT_F32) {
         *reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + at) = make_float4(v[0], v[1], v[2], v[3]);
       } else if constexpr (VEC) {
@@ -196,7 +209,7 @@ __global__ void __launch_bounds__(Q_WARPS * 32) k_fp8_dequantize(Fp8Shape s, con
     } else {
 #pragma unroll
       for (int j = 0; j < P::PER; ++j)
-        if (c + j * P::STEP < s.cols) store_out(out, DT, (uint64_t)(at + j * P::STEP), v[j]);
+        if (c + j * P::STEP < s.cols && CQL_IN(err, at + j * P::STEP, in_out, 407)) store_out(out, DT, (uint64_t)(at + j * P::STEP), v[j]);
     }
   }
 }
@@ -208,7 +221,7 @@ bool vectors_ok(const void* p, int dt, int64_t ld) { return aligned_to(p, 16) &&
 }  // namespace
 
 cudaError_t launch_fp8_quantize(const Fp8Shape& s, const void* src, int dt, int64_t ld, uint8_t* dst, Fp8Launch pdl,
-                                cudaStream_t st) {
+                                uint32_t* err, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((s.rows + Q_WARPS - 1) / Q_WARPS), (unsigned)s.quads);
   cfg.blockDim = dim3(Q_WARPS * 32);
@@ -219,7 +232,7 @@ cudaError_t launch_fp8_quantize(const Fp8Shape& s, const void* src, int dt, int6
   cfg.attrs = at;
   cfg.numAttrs = pdl != kFp8Plain ? 1 : 0;
   const bool vec = vectors_ok(src, dt, ld);
-  auto go = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, s, src, ld, dst, (int)pdl); };
+  auto go = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, s, src, ld, dst, (int)pdl, err); };
   if (dt == CQL_DT_F32) return vec ? go(k_fp8_quantize<CQL_DT_F32, true>) : go(k_fp8_quantize<CQL_DT_F32, false>);
   if (dt == CQL_DT_F16) return vec ? go(k_fp8_quantize<CQL_DT_F16, true>) : go(k_fp8_quantize<CQL_DT_F16, false>);
   return vec ? go(k_fp8_quantize<CQL_DT_BF16, true>) : go(k_fp8_quantize<CQL_DT_BF16, false>);
@@ -293,7 +306,7 @@ cql_status forward(int32_t n_out, int32_t k_in, int32_t experts, const void* wei
       cudaError_t e = few ? ready_fp8_decode() : ready_fp8_gemm();    // before anything is launched
       if (e != cudaSuccess) return CQL_ERR_CUDA;
       e = launch_fp8_quantize(p.x, x, x_dt, ldx, static_cast<uint8_t*>(workspace),
-                                                offsets == nullptr ? kFp8Early : kFp8Offsets, st);
+                                                offsets == nullptr ? kFp8Early : kFp8Offsets, status, st);
       if (e != cudaSuccess) return CQL_ERR_CUDA;
       p.x_base = static_cast<const uint8_t*>(workspace);
     }
@@ -334,7 +347,7 @@ cql_status cql_fp8_quantize(const void* src, cql_dtype dt, int64_t rows, int32_t
   if (!aligned_to(src, esize(dt)) || !aligned_to(matrix, 256)) return CQL_ERR_ALIGN;
   const Fp8Shape s = fp8_shape(rows, cols);
   if (matrix_bytes < s.total) return CQL_ERR_SIZE;
-  return of_cuda(launch_fp8_quantize(s, src, dt, ld, static_cast<uint8_t*>(matrix), kFp8Plain,
+  return of_cuda(launch_fp8_quantize(s, src, dt, ld, static_cast<uint8_t*>(matrix), kFp8Plain, nullptr,
                                      reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -28,9 +28,10 @@ inline Fp8Shape fp8_shape(int64_t rows, int cols) {
 // dst = the block-scaled form of src [rows][ld].  In a forward the kernel is
 // launched programmatically dependent on the one before it and lets the product
 // kernel start: at once, or (where that reads offsets) when those before are done.
+// err: where the checked build records an index out of range, or null.
 enum Fp8Launch { kFp8Plain = 0, kFp8Early = 1, kFp8Offsets = 2 };
 cudaError_t launch_fp8_quantize(const Fp8Shape& s, const void* src, int dt, int64_t ld, uint8_t* dst, Fp8Launch pdl,
-                                cudaStream_t st);
+                                uint32_t* err, cudaStream_t st);
 cudaError_t launch_fp8_dequantize(const Fp8Shape& s, const uint8_t* src, void* out, int dt, int64_t ld,
                                   cudaStream_t st);
 
@@ -52,7 +53,7 @@ struct Fp8Product {
   bool debug;                                // x is withheld, the waits for it run out after ~10 ms
 };
 // Elements from a matrix's first to behind its last, rows ld apart.
-inline uint64_t fp8_extent(int64_t rows, int64_t ld, int cols) { return (uint64_t)((rows - 1) * ld + cols); }
+CQL_HD uint64_t fp8_extent(int64_t rows, int64_t ld, int cols) { return (uint64_t)((rows - 1) * ld + cols); }
 // Few tokens an expert (fp8_decode.cu).  With very few, X is quantised on the
 // way, from `raw`; else it is block-scaled already.
 bool fp8_decodes(int tokens, int experts, int64_t weights);           // weights: n_out * k_in of an expert
