@@ -486,6 +486,15 @@ def _rows_of(name: str, t, cols: Optional[int] = None) -> int:
     return r
 
 
+def _no_gradient(name: str) -> None:
+    """Raise ValueError if autograd would have to see the call: there is no
+    backward pass, and an output without history would drop the gradient."""
+    import torch
+    if torch.is_grad_enabled():
+        raise ValueError(f"{name} requires grad, and the block-scaled FP8 layers have no backward pass: call under "
+                         f"torch.no_grad() or detach {name}")
+
+
 _FP8_TYPES = {}
 
 
@@ -550,7 +559,8 @@ class Fp8Matrix:
     @classmethod
     def quantize(cls, src, stream=None):
         """The block-scaled form of a [rows][cols] fp32/fp16/bf16 CUDA tensor
-        (any distance between rows, adjacent columns)."""
+        (any distance between rows, adjacent columns).  The codes are frozen: no
+        gradient reaches a parameter that they were made from."""
         import torch
         ld = _rows_of("src", src)
         rows, cols = src.shape
@@ -615,7 +625,10 @@ class _Fp8Layer:
     A forward reads the weight before the kernels in front of it are complete:
     after a kernel that writes the layer's weight buffer (other than
     ``cql_fp8_quantize``), some operation that is not a forward has to come first
-    on the stream (``include/cql.h``).  Making the layer contains one."""
+    on the stream (``include/cql.h``).  Making the layer contains one.
+
+    The layers have no backward pass; a forward refuses an x that requires grad
+    while gradients are enabled."""
 
     def __init__(self, weight, n_experts: int, n_out: int, stream=None):
         import torch
@@ -637,6 +650,8 @@ class _Fp8Layer:
             tokens, ldx, x_dt, src, scratch = x.rows, 0, CQL_DT_FP8_BLOCK, x.buffer, 0
         else:
             ldx, src = _rows_of("x", x, self.k_in), x
+            if x.requires_grad:
+                _no_gradient("x")
             tokens, x_dt = x.shape[0], _FP8_TYPES[x.dtype]
             scratch = _fp8_scratch(self.k_in, self.n_experts, tokens)
         if src.device != self.device:
@@ -652,6 +667,8 @@ class _Fp8Layer:
                                  f"{out.dtype}")
             if out.device != self.device:
                 raise ValueError(f"out is on {out.device}, the layer on {self.device}")
+            if out.requires_grad:
+                _no_gradient("out")
             dtype, ldy, y_dt = out.dtype, _rows_of("out", out), _FP8_TYPES[out.dtype]
 
         if stream is None and torch._C._cuda_getDevice() == self._index:          # the common case, straight on
