@@ -405,14 +405,19 @@ cql_status cql_get_device_status(void* workspace, cql_stream_t stream, cql_statu
  * its values, and every output that depends on it, are NaN.
  *
  * In memory (one device buffer, 256-byte aligned, cql_fp8_matrix_layout):
- *   codes   at 0: byte [block][row][128], columns past the last are zero;
+ *   codes   at 0: byte [block][row][128], columns past the last are zero (NaN
+ *           codes in a block that holds an infinity or a NaN);
  *   scales  at scales_off: byte [block / 4][row][block % 4] = e + 127, bytes
  *           of blocks past the last are zero.
  * Both planes are padded with zeros to a multiple of 256 bytes.
  *
  * The forwards compute y = Xq Wq^T from the values above: products and sums in
  * fp32 on the tensor cores (the scales multiply there, exactly), one rounding
- * to y's type.  The result of a call does not depend on other calls or on
+ * to y's type.  The tensor cores truncate where they add to an accumulator, which
+ * takes 2432 columns at most; those sums are added in fp32, rounded to nearest.
+ * Measured with normal x and w, an F32 y is off by 0.4e-7 (1111 columns) to
+ * 2.1e-7 (65536) of itself in the 2-norm, two to three times as far as a plain
+ * fp32 product.  The result of a call does not depend on other calls or on
  * timing.  Buffers of a call must not overlap, except that reads may share. */
 #define CQL_FP8_MAX_ROWS (1 << 24)
 #define CQL_FP8_MAX_COLS 65536

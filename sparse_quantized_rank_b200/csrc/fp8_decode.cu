@@ -36,8 +36,8 @@
 // copied is multiplied: no copy and no commit is under way when a CTA ends.
 //
 // Measured (bf16, calls in a chain, weights not in L2): 11008 x 4096, one token
-// 10.2 us for 45.5 MB, 68 % of the copy bandwidth, reading exactly the weights'
-// bytes from DRAM; 4096 x 11008, 16 tokens 13.1 us, the quantise kernel included;
+// 10.4 us for 45.5 MB, 67 % of the copy bandwidth, reading exactly the weights'
+// bytes from DRAM; 4096 x 11008, 16 tokens 13.0 us, the quantise kernel included;
 // 32 experts of 2048 x 1024, 24 tokens 13.9 us.  With more bytes the share grows
 // (32 experts of 4096 x 4096, 10 tokens each, 545 MB: 83.5 us, 6.5 TB/s): what is
 // left of a small call is its start (launch, barriers and tensor memory, the first
@@ -585,13 +585,21 @@ cudaError_t launch(const Fp8Product& f, DcParams& p, cudaStream_t st) {
 // second time from L2, which small ones still gain from: 2048 x 4096, 64 tokens 9.5
 // and 10.5; 1024 x 4096 7.9 and 10.0; 64 experts of 1024 x 1024 with 64 each 21.5 and
 // 24.6; but 4096 x 4096 11.4 and 10.8, 28672 x 8192 51 and 45.
+// The experts' loads are not known here, their mean is.  This kernel and the pair
+// kernel with loads as 1 / rank, and with every token at one expert:
+//   64 of 1024 x 1024, mean 16  19.0 and 21.2, 11.4 and 11.9; mean 64 24.4 and 27.1, 18.4 and 20.2
+//   32 of 2048 x 2048, mean 16  29.5 and 31.7, 14.8 and 13.6; mean 64 39.0 and 38.2, 25.9 and 23.0
+//   8 of 4096 x 4096,  mean 16  31.6 and 29.7, 15.1 and 12.5; mean 32 30.9 and 32.8, 16.4 and 17.5
 bool fp8_decodes(int tokens, int experts, int64_t weights) {
   const int per = (tokens + experts - 1) / experts;
   return per <= 32 || (per <= 64 && weights <= 8 << 20);
 }
 // Quantising on the way saves a kernel but its time grows with the tokens:
 // 11008 x 4096, 4 tokens 11.6, 8 tokens 12.4 against 11.7 after a quantise
-// kernel, 16 tokens 16.2 against 12.3.
+// kernel, 16 tokens 16.2 against 12.3.  Here too the mean stands for the loads: 32
+// experts of 2048 x 2048, mean 2, even 24.5 against 25.7, as 1 / rank 28.4 against
+// 23.5, every token at one 11.8 against 8.8; 8 of 4096 x 4096, every token at one
+// 20.5 against 12.4.
 bool fp8_decode_quantizes(int tokens, int experts) { return (tokens + experts - 1) / experts <= 4; }
 
 cudaError_t ready_fp8_decode() {

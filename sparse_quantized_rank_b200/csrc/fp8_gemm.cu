@@ -34,9 +34,11 @@
 // over all SMs).  74 tiles of 18944 x 4096 at a time, a block takes 260 ns with
 // zeros as data and 340 ns with random ones: the 1000 W cap lowers the clock, so
 // large products are bound by power (18944 x 4096, 1792 tokens: 96 us, 2900
-// TFLOP/s).  11008 x 4096, 2048 block-scaled tokens: 74 us, 2500 TFLOP/s, the
-// tensor pipe busy for 74 %: six rounds of tiles for 5.8, and some 6 us of start
-// and end.  Few tokens an expert are bound by the weights' bytes: 32 experts of
+// TFLOP/s).  11008 x 4096, 2048 block-scaled tokens: 71 to 77 us, 2500 TFLOP/s (one
+// after another 89, at the power cap).  The busiest pair has six tiles, 86,016
+// cycles of MMA in the 110,000 to 114,000 that the call takes at 1.55 GHz; start and
+// end are some 9,000 of the rest.  For the other 15,000 to 19,000, 10 to 12 us, no
+// cause has been measured.  Few tokens an expert are bound by the weights' bytes: 32 experts of
 // 4096 x 4096, 64 tokens each 92 us, 6.1 TB/s.
 #include <cuda.h>
 
@@ -557,7 +559,12 @@ cudaError_t launch_fp8_gemm(const Fp8Product& f, cudaStream_t st) {
   p.in = {f.w.scales_len / 4, f.x.scales_len / 4, 0, fp8_extent(f.x.rows, f.ldy, f.n)};
   // Token tiles.  A block of a tile takes about 90 + 0.69 nt ns (measured on one
   // pair: 142 ns at nt 64, 173 at 128, 244 at 224), so the cost of a choice is
-  // the number of rounds over the pairs times 130 + nt.
+  // the number of rounds over the pairs times 130 + nt.  The host does not know the
+  // experts' loads: the rule takes them for even and every tile for full.  The copies
+  // are nt tokens wide for every tile; the MMAs of a part-filled one are narrower
+  // (gm_columns), so with uneven loads the true cost is below the rule's and a wider
+  // nt may be the better one (32 experts of 2048 x 2048, 4096 tokens, loads as 1 /
+  // rank: nt 128, 384 tiles, 5.2 rounds; 160 would be 360 tiles, 4.9; not timed).
   const int pairs = device_sm_count() / 2;
   const int per = (p.tok.tokens + f.experts - 1) / f.experts;         // tokens of an expert, evenly loaded
   int64_t best = 0, tiles = 0;

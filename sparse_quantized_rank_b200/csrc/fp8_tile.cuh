@@ -106,9 +106,10 @@ CQL_DEV bool elect_one() {
   return r != 0;
 }
 
-// The two halves of a cluster barrier.  A warp reaches it as a whole: in the forms
-// that let lanes come one by one, warps whose lanes had parted now and then let a
-// barrier complete before every CTA had started.
+// The two halves of a cluster barrier, reached by whole warps.  The forms that let
+// lanes come one by one stood here, behind code where lanes part, when now and then
+// a push went to a CTA that had not started; that a barrier completed early for it
+// is inferred by reading, not shown.
 // cluster_arrive orders no memory accesses (barriers are initialised before it
 // under fence.mbarrier_init).
 CQL_DEV void cluster_arrive() {
